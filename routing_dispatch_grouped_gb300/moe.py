@@ -190,9 +190,15 @@ def _w_dims(w, kind):
     return E, K, (C // 2 if kind == W_GATE_UP else C), 0
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
+def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
+    """A workspace of one call. A call that does not return it names the stream it was given: the
+    block belongs to the current stream, and the allocator would hand it out again while the given
+    one still uses it."""
     # torch's caching allocator returns blocks aligned to at least 512 bytes
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
 
 
 # ------------------------------------------------------------------------------------------------
@@ -784,12 +790,12 @@ def moe_norm(x, weight=None, bias=None, eps=1e-5, rms=False, residual=None, want
 
 @functools.lru_cache(maxsize=256)  # of sizes alone; a call across the C ABI takes a microsecond
 def _norm_backward_bytes(T, d, code):
-    return max(lib().moe_norm_backward_workspace_size(T, d, code), 256)
+    return lib().moe_norm_backward_workspace_size(T, d, code)
 
 
 @functools.lru_cache(maxsize=256)
 def _embed_backward_bytes(T, d):
-    return max(lib().moe_embed_backward_workspace_size(T, d), 256)
+    return lib().moe_embed_backward_workspace_size(T, d)
 
 
 def moe_norm_backward_workspace_size(T, d, dtype) -> int:
@@ -825,8 +831,8 @@ def moe_norm_backward(dy, x, weight, mean, rstd, rms=False, dresidual=None, want
         _ptr(dbias, "dbias", (d,), f32)
     elif want_bias and not rms:
         dbias = torch.empty(d, dtype=f32, device=dev)
-    ws = workspace if workspace is not None else torch.empty(
-        _norm_backward_bytes(T, d, code), dtype=torch.uint8, device=dev)
+    ws = workspace if workspace is not None else _workspace(_norm_backward_bytes(T, d, code), dev,
+                                                            stream)
     st = lib().moe_norm_backward(
         dy.data_ptr(), xp, code, T, d, wp, _CODE[wt], mp, qp, rp, NORM_RMS if rms else 0,
         dx.data_ptr(), None if dweight is None else dweight.data_ptr(),
@@ -888,8 +894,8 @@ def moe_embed_backward(dout, ids, V, scale=1.0, grad_dtype=torch.float32, d_tabl
         _ptr(d_table, "d_table", (V, d), d_table.dtype)
     if _dtype_code(d_table, "d_table") == BF16:
         flags |= WGRAD_BF16
-    ws = workspace if workspace is not None else torch.empty(
-        _embed_backward_bytes(T, d), dtype=torch.uint8, device=dev)
+    ws = workspace if workspace is not None else _workspace(_embed_backward_bytes(T, d), dev,
+                                                            stream)
     st = lib().moe_embed_backward(
         dout.data_ptr(), ip, _dtype_code(dout, "dout"), T, V, d, scale, flags, d_table.data_ptr(),
         ws.data_ptr(), ws.numel(), _current(dout, stream))

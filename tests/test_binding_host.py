@@ -1,0 +1,106 @@
+"""What the binding does around a call of the C ABI, without a GPU: stand-ins for CUDA tensors and
+for the library record what a call is given."""
+import pytest
+import torch
+
+from routing_dispatch_grouped_gb300 import moe
+
+bf16, f32 = torch.bfloat16, torch.float32
+
+
+class Stream:
+    cuda_stream = 0x5157
+
+
+class Cuda:
+    """As much of a contiguous CUDA tensor as the binding looks at."""
+    made = 0
+
+    def __init__(self, shape, dtype, index=0):
+        Cuda.made += 1
+        self.shape, self.dtype, self.index = torch.Size(shape), dtype, index
+        self.device = torch.device("cuda", index)
+        self.is_cuda, self.address, self.streams = True, 0x100000 * Cuda.made, []
+
+    def is_contiguous(self):
+        return True
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return self.address
+
+    def get_device(self):
+        return self.index
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+class Library:
+    """Every call succeeds; the workspaces' sizes are what the real library says."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if name.endswith("_size"):
+            return getattr(moe._lib, name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    moe.lib()
+    fake = Library()
+    monkeypatch.setattr(moe, "lib", lambda: fake)
+    return fake
+
+
+@pytest.fixture
+def allocated(monkeypatch):
+    """The tensors that torch.empty gave out."""
+    got = []
+
+    def empty(*shape, dtype=f32, device=None):
+        got.append(Cuda(shape[0] if isinstance(shape[0], tuple) else shape, dtype))
+        return got[-1]
+    monkeypatch.setattr(torch, "empty", empty)
+    return got
+
+
+def _norm_backward(**kw):
+    T, d = 6, 64
+    x = Cuda((T, d), bf16)
+    return moe.moe_norm_backward(Cuda((T, d), bf16), x, None, Cuda((T,), f32), Cuda((T,), f32),
+                                 dx=Cuda((T, d), bf16), dweight=Cuda((d,), f32),
+                                 dbias=Cuda((d,), f32), **kw)
+
+
+def _embed_backward(**kw):
+    T, V, d = 6, 10, 64
+    return moe.moe_embed_backward(Cuda((T, d), bf16), Cuda((T,), torch.int32), V,
+                                  d_table=Cuda((V, d), f32), **kw)
+
+
+@pytest.mark.parametrize("call", [_norm_backward, _embed_backward])
+def test_a_workspace_of_the_call_is_kept_for_the_stream_it_was_given(library, allocated, call):
+    """Nothing holds such a workspace after the call has returned, so the allocator has to know
+    that the given stream still uses it."""
+    stream = Stream()
+    call(stream=stream)
+    ws, = allocated
+    assert ws.dtype is torch.uint8 and ws.streams == [stream]
+    name, args = library.calls[-1]
+    assert ws.address in args and args[-1] == stream.cuda_stream
