@@ -280,7 +280,8 @@ def moe_gate_up(x_rows, offsets, w_gate_up, sorted_to_slot=None, topk_weights=No
     E, _, I, pk = _w_dims(w_gate_up, W_GATE_UP)
     dev = x_rows.device
     h = h if h is not None else torch.empty(R, I, dtype=x_rows.dtype, device=dev)
-    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev)
+    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev,
+                                                            stream)
     _check("moe_gate_up", lib().moe_gate_up(
         _p(x_rows), _p(offsets), _p(sorted_to_slot), _p(topk_weights), _dt(x_rows), R, d, E, I,
         _p(w_gate_up), (SCALE_INPUT if scale_input else 0) | pk, _p(h), _p(ws), ws.numel(),
@@ -295,7 +296,8 @@ def moe_down(h, offsets, w_down, sorted_to_slot=None, topk_weights=None, fuse_we
     E, _, d, pk = _w_dims(w_down, W_DOWN)
     dev = h.device
     y = y_sorted if y_sorted is not None else torch.empty(R, d, dtype=torch.float32, device=dev)
-    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev)
+    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev,
+                                                            stream)
     _check("moe_down", lib().moe_down(
         _p(h), _p(offsets), _p(sorted_to_slot), _p(topk_weights), _dt(h), R, d, E, I,
         _p(w_down), (FUSE_COMBINE_WEIGHT if fuse_weight else 0) | pk, _p(y), _p(ws), ws.numel(),
@@ -312,7 +314,8 @@ def moe_experts(x_sorted, offsets, w_gate_up, w_down, sorted_to_slot=None, topk_
     dev = x_sorted.device
     h = h if h is not None else torch.empty(R, I, dtype=x_sorted.dtype, device=dev)
     y = y_sorted if y_sorted is not None else torch.empty(R, d, dtype=torch.float32, device=dev)
-    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev)
+    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev,
+                                                            stream)
     _check("moe_experts", lib().moe_experts(
         _p(x_sorted), _p(offsets), _p(sorted_to_slot), _p(topk_weights), _dt(x_sorted), R, d, E,
         I, _p(w_gate_up), _p(w_down), flags, _p(h), _p(y), _p(ws), ws.numel(), _stream(stream)))
@@ -477,7 +480,8 @@ def moe_gate_up_train(x_rows, offsets, w_gate_up, sorted_to_slot=None, topk_weig
     dev = x_rows.device
     h = h if h is not None else torch.empty(R, I, dtype=x_rows.dtype, device=dev)
     ab = ab if ab is not None else torch.empty(R, 2 * I, dtype=x_rows.dtype, device=dev)
-    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev)
+    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev,
+                                                            stream)
     _check("moe_gate_up_train", lib().moe_gate_up_train(
         _p(x_rows), _p(offsets), _p(sorted_to_slot), _p(topk_weights), _dt(x_rows), R, d, E, I,
         _p(w_gate_up), (SCALE_INPUT if scale_input else 0) | pk, _p(h), _p(ab), _p(ws),
@@ -518,7 +522,7 @@ def moe_down_backward(dy_sorted, ab, offsets, w_down, sorted_to_slot=None, topk_
         dw = d_topk_weights if d_topk_weights is not None else torch.empty(
             R, dtype=torch.float32, device=dev)
     ws = workspace if workspace is not None else _workspace(
-        lib().moe_down_backward_workspace_size(R, I, _dt(dy_sorted)), dev)
+        lib().moe_down_backward_workspace_size(R, I, _dt(dy_sorted)), dev, stream)
     _check("moe_down_backward", lib().moe_down_backward(
         _p(dy_sorted), _p(ab), _p(offsets), _p(sorted_to_slot), _p(topk_weights), _dt(dy_sorted),
         R, d, E, I, _p(w_down), (SCALE_INPUT if scale_input else 0) | pk, _p(d_ab), _p(dw),
@@ -533,7 +537,8 @@ def moe_gate_up_backward(d_ab, offsets, w_gate_up, dx_sorted=None, workspace=Non
     E, d, I, pk = _w_dims(w_gate_up, W_GATE_UP)
     dev = d_ab.device
     dx = dx_sorted if dx_sorted is not None else torch.empty(R, d, dtype=torch.float32, device=dev)
-    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev)
+    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev,
+                                                            stream)
     _check("moe_gate_up_backward", lib().moe_gate_up_backward(
         _p(d_ab), _p(offsets), _dt(d_ab), R, d, E, I, _p(w_gate_up), pk, _p(dx), _p(ws),
         ws.numel(), _stream(stream)))
@@ -550,7 +555,8 @@ def moe_weight_grad(a, b, offsets, E, dw=None, workspace=None, stream=None,
     N = b.shape[1]
     dev = a.device
     dw = dw if dw is not None else torch.empty(E, M, N, dtype=out_dtype, device=dev)
-    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev)
+    ws = workspace if workspace is not None else _workspace(moe_experts_workspace_size(), dev,
+                                                            stream)
     if dw.dtype == torch.bfloat16:
         _check("moe_weight_grad_bf16", lib().moe_weight_grad_bf16(
             _p(a), _p(b), _p(offsets), R, M, N, E, _p(dw), _p(ws), ws.numel(), _stream(stream)))

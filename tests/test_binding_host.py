@@ -94,7 +94,30 @@ def _embed_backward(**kw):
                                   d_table=Cuda((V, d), f32), **kw)
 
 
-@pytest.mark.parametrize("call", [_norm_backward, _embed_backward])
+R, d, E, I = 6, 64, 4, 32
+GU, DOWN, OFFSETS = Cuda((E, d, 2 * I), bf16), Cuda((E, I, d), bf16), Cuda((E + 1,), torch.int32)
+STEPS = {
+    "gate_up": lambda **kw: moe.moe_gate_up(Cuda((R, d), bf16), OFFSETS, GU, h=Cuda((R, I), bf16),
+                                            **kw),
+    "down": lambda **kw: moe.moe_down(Cuda((R, I), bf16), OFFSETS, DOWN,
+                                      y_sorted=Cuda((R, d), f32), **kw),
+    "experts": lambda **kw: moe.moe_experts(Cuda((R, d), bf16), OFFSETS, GU, DOWN,
+                                            h=Cuda((R, I), bf16), y_sorted=Cuda((R, d), f32),
+                                            **kw),
+    "gate_up_train": lambda **kw: moe.moe_gate_up_train(
+        Cuda((R, d), bf16), OFFSETS, GU, h=Cuda((R, I), bf16), ab=Cuda((R, 2 * I), bf16), **kw),
+    "down_backward": lambda **kw: moe.moe_down_backward(
+        Cuda((R, d), bf16), Cuda((R, 2 * I), bf16), OFFSETS, DOWN, d_ab=Cuda((R, 2 * I), bf16),
+        **kw),
+    "gate_up_backward": lambda **kw: moe.moe_gate_up_backward(
+        Cuda((R, 2 * I), bf16), OFFSETS, GU, dx_sorted=Cuda((R, d), f32), **kw),
+    "weight_grad": lambda **kw: moe.moe_weight_grad(
+        Cuda((R, d), bf16), Cuda((R, I), bf16), OFFSETS, E, dw=Cuda((E, d, I), f32), **kw),
+}
+
+
+@pytest.mark.parametrize("call", [_norm_backward, _embed_backward, *STEPS.values()],
+                         ids=["norm_backward", "embed_backward", *STEPS])
 def test_a_workspace_of_the_call_is_kept_for_the_stream_it_was_given(library, allocated, call):
     """Nothing holds such a workspace after the call has returned, so the allocator has to know
     that the given stream still uses it."""
@@ -103,4 +126,5 @@ def test_a_workspace_of_the_call_is_kept_for_the_stream_it_was_given(library, al
     ws, = allocated
     assert ws.dtype is torch.uint8 and ws.streams == [stream]
     name, args = library.calls[-1]
+    args = [getattr(a, "value", a) for a in args]
     assert ws.address in args and args[-1] == stream.cuda_stream
