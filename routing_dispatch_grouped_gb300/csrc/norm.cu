@@ -344,6 +344,11 @@ __global__ void __launch_bounds__(THREADS, min_blocks(THREADS, sizeof(T)))
     constexpr int N = Vec<T>::N, P = Vec<T>::P, A = RES ? 3 : 2;
     constexpr bool WARP = THREADS == 32 * kWarps;
     using Sum = RowSum<THREADS, WARP, 2>;
+    // Whether mean(u) goes into u, an instruction less, or, times q, into what is added last. The
+    // first is faster for bf16 rows of up to 10 KB with a residual's gradient (16384 rows of 5120:
+    // 106 us, 120 the other way), the second for the others, by registers (8192 rows of 2880 fp32
+    // values: 49 us, 58 the other way; 4096 of 16384 bf16 values with a residual's: 144 and 177).
+    constexpr bool kMeanInU = RES && sizeof(T) == 2 && THREADS <= 320;
     extern __shared__ uint4 ring[];
     __shared__ __align__(16) float red[Sum::kFloats];
     Share<A, WARP> t(a.T, a.d / N, ring);
@@ -381,8 +386,9 @@ __global__ void __launch_bounds__(THREADS, min_blocks(THREADS, sizeof(T)))
         cp_async_wait<1>();
         uint4 pd[V], px[V];
         f2 t0 = both(0.f), t1 = t0;
-        // xh = x q - mu q
-        const f2 fq = both(q), fmq = both(-mu * q);
+        // The mean is subtracted before q multiplies: x q - mu q, with mu q rounded, would shift the
+        // whole row by up to 2^-25 |mu| q.
+        const f2 fq = both(q), minus_mu = both(-mu);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             pd[i] = t.load(stage, 0, i);
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, min_blocks(THREADS, sizeof(T)))
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const int k = i * P + j;
-                const f2 xh = RMS ? mul(x[j], fq) : fma(x[j], fq, fmq), u = mul(g[j], w[k]);
+                const f2 xh = mul(RMS ? x[j] : add(x[j], minus_mu), fq), u = mul(g[j], w[k]);
                 dw[k] = fma(g[j], xh, dw[k]);
                 t0 = fma(u, xh, t0);
                 if (!RMS) {
@@ -404,8 +410,8 @@ __global__ void __launch_bounds__(THREADS, min_blocks(THREADS, sizeof(T)))
         }
         float v[2] = {halves_sum(t0), RMS ? 0.f : halves_sum(t1)};
         total(v);
-        const f2 c2 = both(-v[0] * inv);
-        const f2 c1q = both(-v[1] * inv * q);
+        const f2 minus_m1 = both(-v[1] * inv), minus_m2 = both(-v[0] * inv);
+        const f2 minus_m1q = both(-v[1] * inv * q);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             keep_packed(pd[i]);
@@ -416,12 +422,15 @@ __global__ void __launch_bounds__(THREADS, min_blocks(THREADS, sizeof(T)))
             if constexpr (RES) Vec<T>::unpack(t.load(stage, 2, i), o);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const f2 xh = RMS ? mul(x[j], fq) : fma(x[j], fq, fmq);
-                const f2 e = fma(xh, c2, mul(g[j], w[i * P + j]));
-                if (RMS)
+                const f2 xh = mul(RMS ? x[j] : add(x[j], minus_mu), fq);
+                if (RMS || kMeanInU) {
+                    const f2 u = RMS ? mul(g[j], w[i * P + j]) : fma(g[j], w[i * P + j], minus_m1);
+                    const f2 e = fma(xh, minus_m2, u);
                     o[j] = RES ? fma(e, fq, o[j]) : mul(e, fq);
-                else
-                    o[j] = RES ? fma(e, fq, add(o[j], c1q)) : fma(e, fq, c1q);
+                } else {
+                    const f2 e = fma(xh, minus_m2, mul(g[j], w[i * P + j]));
+                    o[j] = fma(e, fq, RES ? add(o[j], minus_m1q) : minus_m1q);
+                }
             }
             if (t.ok[i]) dx[t.at + i * t.apart] = Vec<T>::pack(o);
         }
