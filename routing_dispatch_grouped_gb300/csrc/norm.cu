@@ -95,6 +95,14 @@ __device__ __forceinline__ float halves_sum(f2 a) {
     return lo + hi;
 }
 
+// sum / n: the product with 1 / n, and its remainder put right, so that a row of equal values has
+// that value as its mean (sum / n exactly; the product alone misses it for 1000 values, say, and
+// rstd makes the difference large).
+__device__ __forceinline__ float mean_of(float sum, float n, float inv) {
+    const float m = sum * inv;
+    return fmaf(fmaf(-m, n, sum), inv, m);
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
     uint4 u;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
             for (int j = 0; j < V * P; ++j) s = add(s, f[j]);
             v[0] = halves_sum(s);
             total(v);
-            mu = v[0] * inv;
+            mu = mean_of(v[0], (float)a.d, inv);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const f2 minus = both(t.ok[i] ? -mu : 0.f);

@@ -42,3 +42,13 @@ def test_gradient_of_rows_with_a_large_mean(d, dtype, offset):
     c1, c2 = u.mean(1, keepdims=True), (u * xh).mean(1, keepdims=True)
     err = q * (4 * U * u + xh * 46 * U * c2 + 6 * U * xh * c2 + 48 * U * c1)
     assert np.all(np.abs(f64(dx) - rx) <= OUT[dtype] * np.abs(rx) + err)
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+def test_a_row_of_equal_values_is_its_own_mean(dtype):
+    """Whatever the width: the sum of a row of one such value is exact, and so is its quotient."""
+    values = torch.tensor([1000.0, -100.5, 7.25, 0.1875], device=DEV, dtype=dtype)
+    for d in [*range(8, 2048, 8), 5000, 7000, 8192]:
+        x = values[:, None].expand(-1, d).contiguous()
+        y, _, mean, _ = moe.moe_norm(x)
+        assert torch.equal(mean, values.float()) and not y.any(), d
