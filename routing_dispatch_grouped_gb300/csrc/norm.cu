@@ -18,6 +18,8 @@ constexpr int kWarps = 8;            // warps of a block in that form
 constexpr int V = 2;                 // 16-byte vectors of a row in a thread's hands
 constexpr int kStages = 2;           // rows a thread group has in flight or in hand
 constexpr int kFlight = 30 << 10;    // bytes of rows on their way to an SM in the forward pass
+constexpr float kInfinity = __builtin_huge_valf();
+constexpr float kLeastVar = 1e-30f;  // squares that count lose digits below it (fp32's range ends)
 
 template <typename T>
 struct Vec;  // 16 bytes of a row as pairs of fp32 values
@@ -235,8 +237,11 @@ struct Share {
 // starting and draining count for more; 8 rows of 2048: 1.8 us, latency alone. The layer norm's
 // two sums over a row are taken one after the other (the squares about the mean, so that a large
 // mean costs no precision); the second costs 2 us of those 24.2.
+// The bound on blocks holds the registers at 64 (80 where a warp takes a row): the rare second
+// pass over a row out of range would have 82 otherwise. It costs other rows 0 to 2%.
 template <typename T, int THREADS, bool RMS, bool RES>
-__global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : THREADS == 256 ? 3 : 1)
+    norm_kernel(const NormArgs a) {
     constexpr int N = Vec<T>::N, P = Vec<T>::P, A = RES ? 2 : 1;
     constexpr bool WARP = THREADS == 32 * kWarps;
     using Sum = RowSum<THREADS, WARP, 1>;
@@ -278,27 +283,56 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
                 Vec<T>::unpack(u, f + i * P);  // the norm sees the stored sum
             }
         }
-        float mu = 0.f, v[1];
-        f2 s = both(0.f);
-        if constexpr (!RMS) {
+        // f less its mean mu; returns the sum of its squares.
+        float mu = 0.f;
+        auto centre = [&] {
+            float v[1];
+            f2 s = both(0.f);
+            if constexpr (!RMS) {
 #pragma unroll
-            for (int j = 0; j < V * P; ++j) s = add(s, f[j]);
+                for (int j = 0; j < V * P; ++j) s = add(s, f[j]);
+                v[0] = halves_sum(s);
+                total(v);
+                mu = mean_of(v[0], (float)a.d, inv);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const f2 minus = both(t.ok[i] ? -mu : 0.f);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) f[i * P + j] = add(f[i * P + j], minus);
+                }
+                s = both(0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < V * P; ++j) s = fma(f[j], f[j], s);
             v[0] = halves_sum(s);
             total(v);
-            mu = mean_of(v[0], (float)a.d, inv);
+            return v[0];
+        };
+        float var = fmaf(centre(), inv, a.eps), q = 1.f / sqrtf(var), rstd = q;
+        // Squares (or the sum) beyond fp32, or below it with an eps of next to nothing: once more
+        // with the row scaled by a power of two. What is not finite then holds NaN or an infinity.
+        // All threads of a row have the same var.
+        if (__builtin_expect(!(var >= kLeastVar && var < kInfinity), 0)) {
+            const bool small = var < kLeastVar;
+            const float up = small ? 0x1p96f : 0x1p-100f, down = small ? 0x1p-96f : 0x1p100f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const f2 minus = both(t.ok[i] ? -mu : 0.f);
+                Vec<T>::unpack(t.load(stage, 0, i), f + i * P);
+                if constexpr (RES) {
+                    f2 r[P];
+                    Vec<T>::unpack(t.load(stage, 1, i), r);
 #pragma unroll
-                for (int j = 0; j < P; ++j) f[i * P + j] = add(f[i * P + j], minus);
+                    for (int j = 0; j < P; ++j) f[i * P + j] = add(f[i * P + j], r[j]);
+                    Vec<T>::unpack(Vec<T>::pack(f + i * P), f + i * P);
+                }
+#pragma unroll
+                for (int j = 0; j < P; ++j) f[i * P + j] = mul(f[i * P + j], both(up));
             }
-            s = both(0.f);
+            var = fmaf(centre(), inv, a.eps * up * up);
+            q = var < kInfinity ? 1.f / sqrtf(var) : __int_as_float(0x7fffffff);
+            rstd = q * up;
+            mu *= down;
         }
-#pragma unroll
-        for (int j = 0; j < V * P; ++j) s = fma(f[j], f[j], s);
-        v[0] = halves_sum(s);
-        total(v);
-        const float q = 1.f / sqrtf(fmaf(v[0], inv, a.eps));
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             f2 o[P];
@@ -311,7 +345,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
         }
         if (t.gt == 0) {
             if (!RMS && a.mean) a.mean[t.row] = mu;
-            if (a.rstd) a.rstd[t.row] = q;
+            if (a.rstd) a.rstd[t.row] = rstd;
         }
         const uint32_t was = stage;
         stage = other;

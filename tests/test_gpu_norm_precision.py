@@ -52,3 +52,64 @@ def test_a_row_of_equal_values_is_its_own_mean(dtype):
         x = values[:, None].expand(-1, d).contiguous()
         y, _, mean, _ = moe.moe_norm(x)
         assert torch.equal(mean, values.float()) and not y.any(), d
+
+
+def _bound(s, w, b, mu, q, y, dtype, rms):
+    """A row's sums are trees of at most 40 additions, so its mean is off by 40 U mean|s|, rstd by
+    half of that relatively, the squares' error and its own roundings."""
+    dmu = np.zeros(s.shape[0]) if rms else 42 * U * np.abs(s).mean(1) + U * np.abs(mu)
+    xw = np.abs(s - mu[:, None]) * q[:, None] * np.abs(w)
+    dq = 50 * U + (dmu * q) ** 2
+    return (OUT[dtype] * np.abs(y) + (dq[:, None] + 4 * U) * xw + 2 * U * np.abs(b) +
+            (q * dmu)[:, None] * np.abs(w) +
+            2 * U * q[:, None] * np.abs(w) * (np.abs(s) + np.abs(mu)[:, None]))
+
+
+def _check_rows(x, residual, w, b, eps, rms, rows):
+    """`rows` of moe_norm against the definition."""
+    y, total, mean, rstd = moe.moe_norm(x, w, None if rms else b, eps, rms=rms, residual=residual)
+    s = f64(x if residual is None else total)[rows]
+    w64, b64 = f64(w), np.zeros(x.shape[1]) if rms else f64(b)
+    ref, mu, q = S.norm(s, w64, b64, eps, rms)
+    assert np.all(np.abs(f64(y)[rows] - ref) <= _bound(s, w64, b64, mu, q, ref, x.dtype, rms))
+    # rstd is a fp32 number, which may be a subnormal one
+    dmu = 0 if rms else 42 * U * np.abs(s).mean(1) + U * np.abs(mu)
+    assert np.all(np.abs(f64(rstd)[rows] - q) <= q * (52 * U + (dmu * q) ** 2) + 2.0 ** -149)
+    if not rms:
+        assert np.all(np.abs(f64(mean)[rows] - mu) <= dmu)
+    return y, mean, rstd
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("d,dtype", SHAPES + [(1000, bf16), (1000, f32)])
+def test_rows_beyond_the_squares_range(d, dtype, residual, rms):
+    """Infinities and NaN make their whole row NaN, in both forms; finite rows stay right however
+    large; the rows beside them are untouched."""
+    w, b = _normal((d,), f32, "w", 0.3) + 1, _normal((d,), f32, "b", 0.3)
+    x = _normal((12, d), f32, "x")
+    x[1, d // 2], x[2, 0], x[3, d - 1] = float("inf"), -float("inf"), float("nan")
+    x[4] *= 1e19                                       # squares above the range, one by one
+    x[5] = x[5] * 1e36 + 3e37
+    x[6] = 3.3e38 * (1 - (torch.arange(d, device=DEV) % 7) / 64)     # so is the sum
+    x[7] = 3.3e38 * torch.sign(x[7])                   # and the distance from the mean
+    x[8, 3] = 1e30                                     # one large entry
+    x[9] *= 2e-10
+    x = x.to(dtype)
+    r = None
+    if residual:                                       # x / 2 + x / 2: the same rows
+        x = x / 2
+        r = x.clone()
+    y, mean, rstd = _check_rows(x, r, w, b, 1e-5, rms, [0, 4, 5, 6, 7, 8, 9, 10, 11])
+    assert y[1:4].isnan().all() and rstd[1:4].isnan().all()
+    assert rms or not mean[1:4].isfinite().any()
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("d,dtype", SHAPES)
+def test_small_rows_without_an_epsilon(d, dtype, rms):
+    w, b = _normal((d,), f32, "w", 0.3) + 1, _normal((d,), f32, "b", 0.3)
+    sizes = torch.tensor([1.0, 1e-14, 1e-16, 1e-20, 1e-25, 1e-32], device=DEV)
+    x = (_normal((6, d), f32, "x") * sizes[:, None]).to(dtype)
+    _check_rows(x, None, w, b, 0.0, rms, list(range(6)))
+    _check_rows(x, None, w, b, 1e-38, rms, list(range(6)))
