@@ -189,6 +189,18 @@ moe_status clear_status(void* workspace, cudaStream_t s) {
     return launch_status(cudaMemsetAsync(workspace, 0, sizeof(int), s));
 }
 
+// The status word of an empty call. Such a call succeeds on any machine, so the word is written only
+// where the driver knows the workspace for device memory.
+moe_status clear_status_of_empty(void* workspace, cudaStream_t s) {
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, workspace) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_OK;
+    }
+    const bool device = a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged;
+    return device ? clear_status(workspace, s) : MOE_OK;
+}
+
 moe_status run_gemm(GemmKind kind, const void* a, const void* b, bool packed,
                     const int32_t* offsets, const int32_t* s2p, const float* w, bool scale,
                     moe_dtype dt, int R, int K, int N, int E, void* out, int* status,
@@ -1483,6 +1495,8 @@ moe_status moe_norm_backward(const void* dy, const void* x, moe_dtype dt, int T,
         return MOE_ERR_WORKSPACE;
     cudaStream_t s = (cudaStream_t)stream;
     if (T == 0) {  // sums over no rows
+        const moe_status st = clear_status_of_empty(workspace, s);
+        if (st != MOE_OK) return st;
         cudaError_t e = cudaSuccess;
         if (dweight) e = cudaMemsetAsync(dweight, 0, (size_t)d * 4, s);
         if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, (size_t)d * 4, s);
@@ -1505,10 +1519,10 @@ moe_status moe_embed(const void* ids, const void* table, moe_dtype dt, int T, in
     if (T >= kEmbedMaxTokens) return MOE_ERR_UNSUPPORTED;
     if (workspace ? !aligned256(workspace) || ws_bytes < kStatusBytes : ws_bytes != 0)
         return MOE_ERR_WORKSPACE;
-    if (T == 0) return MOE_OK;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (T == 0) return workspace ? clear_status_of_empty(workspace, s) : MOE_OK;
     if (!ids || !table || !out) return MOE_ERR_INVALID_ARG;
     if (!aligned16(ids) || !aligned16(table) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
-    cudaStream_t s = (cudaStream_t)stream;
     if (workspace && T > kEmbedCheckTokens) {  // fewer: one block of the kernel writes the status word
         const moe_status st = clear_status(workspace, s);
         if (st != MOE_OK) return st;
