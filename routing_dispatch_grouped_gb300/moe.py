@@ -724,10 +724,16 @@ def forward_train_workspace_views(ws: torch.Tensor, T, d, E, k, I, Is, dtype):
 _CODE = {torch.float32: F32, torch.bfloat16: BF16}
 
 
-def _current(t, stream):
-    """The stream's handle: the one given, or the current one of t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None \
-        else stream.cuda_stream
+def _device(t, name):
+    """The current device, on which the library launches and where every tensor has to be."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return torch._C._cuda_getDevice()
+
+
+def _current(dev, stream):
+    """The stream's handle: the one given, or the current one of the current device."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _dtype_code(t, name):
@@ -737,20 +743,25 @@ def _dtype_code(t, name):
     return code
 
 
-def _ptr(t, name, shape, dtype):
-    """t's address (None for None): a contiguous CUDA tensor of this shape and dtype."""
+def _look(t, name, dev):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on the current device")
+
+
+def _ptr(t, name, shape, dtype, dev):
+    """t's address (None for None): a contiguous tensor on dev of this shape and dtype."""
     if t is None:
         return None
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    _look(t, name, dev)
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must have shape {tuple(shape)} and dtype {dtype}")
     return t.data_ptr()
 
 
-def _rows(t, name):
-    if not (t.is_cuda and t.is_contiguous()) or t.dim() != 2:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of two dimensions")
+def _rows(t, name, dev):
+    _look(t, name, dev)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
     return t.shape
 
 
@@ -759,7 +770,8 @@ def moe_norm(x, weight=None, bias=None, eps=1e-5, rms=False, residual=None, want
     """Layer norm (rms: root-mean-square norm) of x + residual; weight and bias float32 or
     bfloat16. Returns (y, sum, mean, rstd): sum is None without a residual, mean with rms, both
     statistics without want_stats (unless they were given)."""
-    shape = _rows(x, "x")
+    dev = _device(x, "x")
+    shape = _rows(x, "x", dev)
     T, d = shape
     dtype = x.dtype
     code = _dtype_code(x, "x")
@@ -767,35 +779,36 @@ def moe_norm(x, weight=None, bias=None, eps=1e-5, rms=False, residual=None, want
         (bias if weight is None else weight).dtype
     if wt not in _CODE:
         raise TypeError(f"unsupported dtype {wt} of weight or bias")
-    wp, bp = _ptr(weight, "weight", (d,), wt), _ptr(bias, "bias", (d,), wt)
-    rp = _ptr(residual, "residual", shape, dtype)
+    wp, bp = _ptr(weight, "weight", (d,), wt, dev), _ptr(bias, "bias", (d,), wt, dev)
+    rp = _ptr(residual, "residual", shape, dtype, dev)
     if y is None:
         y = torch.empty_like(x)
     else:
-        _ptr(y, "y", shape, dtype)
+        _ptr(y, "y", shape, dtype, dev)
     if sum is not None:
-        _ptr(sum, "sum", shape, dtype)
+        _ptr(sum, "sum", shape, dtype, dev)
     elif residual is not None:
         sum = torch.empty_like(x)
     if mean is not None:
-        _ptr(mean, "mean", (T,), torch.float32)
+        _ptr(mean, "mean", (T,), torch.float32, dev)
     elif want_stats and not rms:
         mean = torch.empty(T, dtype=torch.float32, device=x.device)
     if rstd is not None:
-        _ptr(rstd, "rstd", (T,), torch.float32)
+        _ptr(rstd, "rstd", (T,), torch.float32, dev)
     elif want_stats:
         rstd = torch.empty(T, dtype=torch.float32, device=x.device)
     st = lib().moe_norm(x.data_ptr(), rp, code, T, d, wp, bp, _CODE[wt], eps,
                         NORM_RMS if rms else 0, None if sum is None else sum.data_ptr(),
                         y.data_ptr(), None if mean is None else mean.data_ptr(),
-                        None if rstd is None else rstd.data_ptr(), _current(x, stream))
+                        None if rstd is None else rstd.data_ptr(), _current(dev, stream))
     if st:
         raise MoEError("moe_norm", st)
     return y, sum, mean, rstd
 
 
-@functools.lru_cache(maxsize=256)  # of sizes alone; a call across the C ABI takes a microsecond
-def _norm_backward_bytes(T, d, code):
+# of sizes and the device (its SM count) alone; a call across the C ABI takes a microsecond
+@functools.lru_cache(maxsize=256)
+def _norm_backward_bytes(T, d, code, dev):
     return lib().moe_norm_backward_workspace_size(T, d, code)
 
 
@@ -814,45 +827,46 @@ def moe_norm_backward(dy, x, weight, mean, rstd, rms=False, dresidual=None, want
     """Gradient of moe_norm; x is what was normed (moe_norm's sum if it had a residual), mean and
     rstd its statistics (mean None with rms). Returns (dx, dweight, dbias): dbias is None with
     rms."""
-    shape = _rows(dy, "dy")
+    dev = _device(dy, "dy")
+    shape = _rows(dy, "dy", dev)
     T, d = shape
-    dtype, dev, f32 = dy.dtype, dy.device, torch.float32
+    dtype, f32 = dy.dtype, torch.float32
     code = _dtype_code(dy, "dy")
-    xp = _ptr(x, "x", shape, dtype)
+    xp = _ptr(x, "x", shape, dtype, dev)
     wt = f32 if weight is None else weight.dtype
     if wt not in _CODE:
         raise TypeError(f"unsupported dtype {wt} of weight")
-    wp = _ptr(weight, "weight", (d,), wt)
-    mp, qp = _ptr(mean, "mean", (T,), f32), _ptr(rstd, "rstd", (T,), f32)
-    rp = _ptr(dresidual, "dresidual", shape, dtype)
+    wp = _ptr(weight, "weight", (d,), wt, dev)
+    mp, qp = _ptr(mean, "mean", (T,), f32, dev), _ptr(rstd, "rstd", (T,), f32, dev)
+    rp = _ptr(dresidual, "dresidual", shape, dtype, dev)
     if dx is None:
         dx = torch.empty_like(dy)
     else:
-        _ptr(dx, "dx", shape, dtype)
+        _ptr(dx, "dx", shape, dtype, dev)
     if dweight is not None:
-        _ptr(dweight, "dweight", (d,), f32)
+        _ptr(dweight, "dweight", (d,), f32, dev)
     elif want_weight:
-        dweight = torch.empty(d, dtype=f32, device=dev)
+        dweight = torch.empty(d, dtype=f32, device=dy.device)
     if dbias is not None:
-        _ptr(dbias, "dbias", (d,), f32)
+        _ptr(dbias, "dbias", (d,), f32, dev)
     elif want_bias and not rms:
-        dbias = torch.empty(d, dtype=f32, device=dev)
-    ws = workspace if workspace is not None else _workspace(_norm_backward_bytes(T, d, code), dev,
-                                                            stream)
+        dbias = torch.empty(d, dtype=f32, device=dy.device)
+    ws = workspace if workspace is not None else _workspace(
+        _norm_backward_bytes(T, d, code, dev), dy.device, stream)
+    _look(ws, "workspace", dev)
     st = lib().moe_norm_backward(
         dy.data_ptr(), xp, code, T, d, wp, _CODE[wt], mp, qp, rp, NORM_RMS if rms else 0,
         dx.data_ptr(), None if dweight is None else dweight.data_ptr(),
         None if dbias is None else dbias.data_ptr(), ws.data_ptr(), ws.numel(),
-        _current(dy, stream))
+        _current(dev, stream))
     if st:
         raise MoEError("moe_norm_backward", st)
     return dx, dweight, dbias
 
 
-def _ids(ids):
+def _ids(ids, dev):
     """(address, flag) of int32 or int64 token ids."""
-    if not (ids.is_cuda and ids.is_contiguous()):
-        raise ValueError("ids must be a contiguous CUDA tensor")
+    _look(ids, "ids", dev)
     if ids.dtype is torch.int64:
         return ids.data_ptr(), IDS_64
     if ids.dtype is not torch.int32:
@@ -864,17 +878,21 @@ def moe_embed(ids, table, scale=1.0, out=None, workspace=None, stream=None):
     """scale * table[ids] for int32 or int64 ids of any shape; returns [*ids.shape, d]. An id
     outside the table gives a row of zeros; with a workspace (uint8, 256 bytes) its status word says
     so."""
-    ip, flags = _ids(ids)
-    V, d = _rows(table, "table")
-    dtype, dev = table.dtype, table.device
+    dev = _device(table, "table")
+    ip, flags = _ids(ids, dev)
+    V, d = _rows(table, "table", dev)
+    dtype = table.dtype
     code = _dtype_code(table, "table")
     if out is None:
-        out = torch.empty((*ids.shape, d), dtype=dtype, device=dev)
+        out = torch.empty((*ids.shape, d), dtype=dtype, device=table.device)
     else:
-        _ptr(out, "out", (*ids.shape, d), dtype)
-    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+        _ptr(out, "out", (*ids.shape, d), dtype, dev)
+    wp, wb = None, 0
+    if workspace is not None:
+        _look(workspace, "workspace", dev)
+        wp, wb = workspace.data_ptr(), workspace.numel()
     st = lib().moe_embed(ip, table.data_ptr(), code, ids.numel(), V, d, scale, flags,
-                         out.data_ptr(), wp, wb, _current(table, stream))
+                         out.data_ptr(), wp, wb, _current(dev, stream))
     if st:
         raise MoEError("moe_embed", st)
     return out
@@ -888,23 +906,24 @@ def moe_embed_backward(dout, ids, V, scale=1.0, grad_dtype=torch.float32, d_tabl
                        workspace=None, stream=None):
     """Gradient of moe_embed with respect to the table: [V, d] of grad_dtype (float32 or
     bfloat16; d_table's own when given), rows without a token zero."""
-    ip, flags = _ids(ids)
-    if not (dout.is_cuda and dout.is_contiguous()):
-        raise ValueError("dout must be a contiguous CUDA tensor")
+    dev = _device(dout, "dout")
+    ip, flags = _ids(ids, dev)
+    _look(dout, "dout", dev)
     if dout.shape[:-1] != ids.shape:
         raise ValueError("dout must have one row for each id")
-    d, T, dev = dout.shape[-1], ids.numel(), dout.device
+    d, T = dout.shape[-1], ids.numel()
     if d_table is None:
-        d_table = torch.empty(V, d, dtype=grad_dtype, device=dev)
+        d_table = torch.empty(V, d, dtype=grad_dtype, device=dout.device)
     else:
-        _ptr(d_table, "d_table", (V, d), d_table.dtype)
+        _ptr(d_table, "d_table", (V, d), d_table.dtype, dev)
     if _dtype_code(d_table, "d_table") == BF16:
         flags |= WGRAD_BF16
-    ws = workspace if workspace is not None else _workspace(_embed_backward_bytes(T, d), dev,
-                                                            stream)
+    ws = workspace if workspace is not None else _workspace(_embed_backward_bytes(T, d),
+                                                            dout.device, stream)
+    _look(ws, "workspace", dev)
     st = lib().moe_embed_backward(
         dout.data_ptr(), ip, _dtype_code(dout, "dout"), T, V, d, scale, flags, d_table.data_ptr(),
-        ws.data_ptr(), ws.numel(), _current(dout, stream))
+        ws.data_ptr(), ws.numel(), _current(dev, stream))
     if st:
         raise MoEError("moe_embed_backward", st)
     return d_table
@@ -933,14 +952,14 @@ def adamw_state(param, bits=32):
 
 # a property of every tensor of a list, without a Python frame for each
 _T = torch.Tensor
-_dtype_of, _is_cuda = _T.dtype.__get__, _T.is_cuda.__get__
+_dtype_of, _device_of = _T.dtype.__get__, _T.get_device
 
 
-def _column(ts, name, counts, dtype):
-    """Addresses of a list of contiguous CUDA tensors with these element counts and one dtype (each
-    None: not looked at)."""
-    if not (all(map(_is_cuda, ts)) and all(map(_T.is_contiguous, ts))):
-        raise ValueError(f"{name} must be contiguous CUDA tensors")
+def _column(ts, name, counts, dtype, dev):
+    """Addresses of a list of contiguous tensors on dev with these element counts and one dtype
+    (each None: not looked at)."""
+    if set(map(_device_of, ts)) != {dev} or not all(map(_T.is_contiguous, ts)):
+        raise ValueError(f"{name} must be contiguous CUDA tensors on the current device")
     if counts is not None and list(map(_T.numel, ts)) != counts:
         raise ValueError(f"{name} must have their parameters' element counts")
     if dtype is not None and set(map(_dtype_of, ts)) != {dtype}:
@@ -975,12 +994,13 @@ def moe_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, beta1=0.9, be
     for x in (grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales, decay):
         if x is not None and len(x) != n:
             raise ValueError("the lists must have one length")
+    dev = _device(params[0], "params")
     counts = list(map(_T.numel, params))
     # moe_adamw_tensor as ten 64-bit words: seven addresses, n, the two dtypes, weight_decay
     words = [0] * (10 * n)
     for k, (xs, name) in enumerate(((params, "params"), (grads, "grads"), (exp_avgs, "exp_avgs"),
                                     (exp_avg_sqs, "exp_avg_sqs"))):
-        words[k::10] = _column(xs, name, counts if k else None, None)
+        words[k::10] = _column(xs, name, counts if k else None, None, dev)
     eight = _where(exp_avg_scales)
     if eight != _where(exp_avg_sq_scales):
         raise ValueError("exp_avg_scales and exp_avg_sq_scales must go together")
@@ -988,7 +1008,8 @@ def moe_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, beta1=0.9, be
         blocks = [-(-counts[i] // ADAMW_BLOCK) for i in eight]
         for k, xs, name in ((4, exp_avg_scales, "exp_avg_scales"),
                             (5, exp_avg_sq_scales, "exp_avg_sq_scales")):
-            for i, p in zip(eight, _column([xs[i] for i in eight], name, blocks, torch.float32)):
+            for i, p in zip(eight, _column([xs[i] for i in eight], name, blocks, torch.float32,
+                                           dev)):
                 words[10 * i + k] = p
     for xs, name in ((exp_avgs, "exp_avgs"), (exp_avg_sqs, "exp_avg_sqs")):
         if eight:
@@ -1001,16 +1022,16 @@ def moe_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, beta1=0.9, be
     copied = _where(copies)
     if copied:
         for i, p in zip(copied, _column([copies[i] for i in copied], "copies",
-                                        [counts[i] for i in copied], torch.bfloat16)):
+                                        [counts[i] for i in copied], torch.bfloat16, dev)):
             words[10 * i + 6] = p
     words[7::10] = counts
     words[8::10] = [p | g << 32 for p, g in zip(_codes(params, "params"), _codes(grads, "grads"))]
     bits = {w: struct.unpack("<q", struct.pack("<d", w))[0] for w in set(decay)}
     words[9::10] = map(bits.__getitem__, decay)
     st = lib().moe_adamw(struct.pack(f"{10 * n}q", *words), n, lr, beta1, beta2, eps, step,
-                         _ptr(schedule, "schedule", (3,), torch.float32),
-                         _ptr(grad_scale, "grad_scale", (1,), torch.float32),
-                         _current(params[0], stream))
+                         _ptr(schedule, "schedule", (3,), torch.float32, dev),
+                         _ptr(grad_scale, "grad_scale", (1,), torch.float32, dev),
+                         _current(dev, stream))
     if st:
         raise MoEError("moe_adamw", st)
 

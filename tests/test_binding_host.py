@@ -80,6 +80,12 @@ def allocated(monkeypatch):
     return got
 
 
+@pytest.fixture(autouse=True)
+def device_0(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0)
+
+
 def _norm_backward(**kw):
     T, d = 6, 64
     x = Cuda((T, d), bf16)
@@ -128,3 +134,91 @@ def test_a_workspace_of_the_call_is_kept_for_the_stream_it_was_given(library, al
     name, args = library.calls[-1]
     args = [getattr(a, "value", a) for a in args]
     assert ws.address in args and args[-1] == stream.cuda_stream
+
+
+# ------------------------------------------------------------------------------------------------
+# The library launches on the current device: a tensor on another one is refused before the call.
+# ------------------------------------------------------------------------------------------------
+def _operands(call):
+    """The stand-ins of a call by name, on device 0."""
+    T, V, d = 6, 10, 64
+    rows, stat, param = ((T, d), bf16), ((T,), f32), ((d,), f32)
+    return {k: Cuda(*v) for k, v in {
+        "moe_norm": dict(x=rows, weight=param, bias=param, residual=rows, y=rows, sum=rows,
+                         mean=stat, rstd=stat),
+        "moe_norm_backward": dict(dy=rows, x=rows, weight=param, mean=stat, rstd=stat,
+                                  dresidual=rows, dx=rows, dweight=param, dbias=param,
+                                  workspace=((1 << 20,), torch.uint8)),
+        "moe_embed": dict(ids=((T,), torch.int32), table=((V, d), bf16), out=rows,
+                          workspace=((256,), torch.uint8)),
+        "moe_embed_backward": dict(dout=rows, ids=((T,), torch.int32), d_table=((V, d), f32),
+                                   workspace=((1 << 20,), torch.uint8)),
+    }[call].items()}
+
+
+@pytest.mark.parametrize("call", ["moe_norm", "moe_norm_backward", "moe_embed",
+                                  "moe_embed_backward"])
+def test_a_tensor_on_another_device_is_refused(library, monkeypatch, call):
+    more = dict(V=10) if call == "moe_embed_backward" else {}
+    ops = _operands(call)
+    getattr(moe, call)(**ops, **more)
+    assert len(library.calls) == 1
+    for name in ops:
+        ops = _operands(call)
+        ops[name].index = 1
+        with pytest.raises(ValueError, match=name):
+            getattr(moe, call)(**ops, **more)
+    # all of them on a device that is not the current one
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    with pytest.raises(ValueError, match="device"):
+        getattr(moe, call)(**_operands(call), **more)
+    assert len(library.calls) == 1
+
+
+def test_a_workspace_size_is_kept_by_device(monkeypatch):
+    class Sizes:
+        """A library on devices of 100 and 200 SMs."""
+        def moe_norm_backward_workspace_size(self, T, d, code):
+            return 100 * (torch._C._cuda_getDevice() + 1)
+    monkeypatch.setattr(moe, "lib", Sizes)
+    moe._norm_backward_bytes.cache_clear()
+    got = []
+    for dev in (0, 1, 0):
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: dev)
+        got.append(moe._norm_backward_bytes(7, 64, 1, dev))
+    moe._norm_backward_bytes.cache_clear()
+    assert got == [100, 200, 100]
+
+
+def _adamw(monkeypatch, moments=f32, scales=False, elsewhere=None):
+    """moe_adamw on three tensors of 300 elements (host memory: only its addresses are taken);
+    elsewhere: (argument, index) of the one on another device."""
+    n = 3
+
+    def column(dtype, size=300):
+        return [torch.zeros(size).to(dtype) for _ in range(n)]
+    kw = dict(params=column(f32), grads=column(bf16), exp_avgs=column(moments),
+              exp_avg_sqs=column(moments), copies=column(bf16), schedule=torch.zeros(3),
+              grad_scale=torch.zeros(1))
+    if scales:
+        kw.update(exp_avg_scales=column(f32, 2), exp_avg_sq_scales=column(f32, 2))
+    odd = None
+    if elsewhere:
+        odd = kw[elsewhere[0]]
+        odd = odd[elsewhere[1]] if isinstance(odd, list) else odd
+    monkeypatch.setattr(moe, "_device", lambda t, name: 0)
+    monkeypatch.setattr(moe, "_device_of", lambda t: int(t is odd))
+    monkeypatch.setattr(moe, "_look", lambda t, name, dev: None)
+    return moe.moe_adamw(step=1, **kw)
+
+
+@pytest.mark.parametrize("name", ["params", "grads", "exp_avgs", "exp_avg_sqs", "copies",
+                                  "exp_avg_scales", "exp_avg_sq_scales"])
+def test_adamw_refuses_a_list_over_several_devices(library, monkeypatch, name):
+    kw = dict(moments=torch.float8_e4m3fn, scales=True)
+    _adamw(monkeypatch, **kw)
+    assert len(library.calls) == 1
+    for i in range(3):
+        with pytest.raises(ValueError, match=name):
+            _adamw(monkeypatch, **kw, elsewhere=(name, i))
+    assert len(library.calls) == 1
