@@ -953,6 +953,7 @@ def adamw_state(param, bits=32):
 # a property of every tensor of a list, without a Python frame for each
 _T = torch.Tensor
 _dtype_of, _device_of = _T.dtype.__get__, _T.get_device
+_E4M3 = {torch.float8_e4m3fn, torch.uint8}  # the numbers, or their bytes
 
 
 def _column(ts, name, counts, dtype, dev):
@@ -1014,8 +1015,8 @@ def moe_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, beta1=0.9, be
     for xs, name in ((exp_avgs, "exp_avgs"), (exp_avg_sqs, "exp_avg_sqs")):
         if eight:
             small = set(eight)
-            if any(xs[i].element_size() != 1 for i in eight):
-                raise TypeError(f"{name} with scales must be 8-bit")
+            if not {xs[i].dtype for i in eight} <= _E4M3:
+                raise TypeError(f"{name} with scales must be float8_e4m3fn (or its bytes, uint8)")
             xs = [x for i, x in enumerate(xs) if i not in small]
         if set(map(_dtype_of, xs)) - {torch.float32}:
             raise TypeError(f"{name} must be float32, or 8-bit with scales")

@@ -222,3 +222,14 @@ def test_adamw_refuses_a_list_over_several_devices(library, monkeypatch, name):
         with pytest.raises(ValueError, match=name):
             _adamw(monkeypatch, **kw, elsewhere=(name, i))
     assert len(library.calls) == 1
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.int8, torch.bool, f32])
+def test_adamw_refuses_8_bit_moments_of_another_kind(library, monkeypatch, dtype):
+    """E5M2 numbers or integers would be read as E4M3 numbers."""
+    for good in (torch.float8_e4m3fn, torch.uint8):
+        _adamw(monkeypatch, moments=good, scales=True)
+    assert len(library.calls) == 2
+    with pytest.raises(TypeError, match="exp_avgs"):
+        _adamw(monkeypatch, moments=dtype, scales=True)
+    assert len(library.calls) == 2
