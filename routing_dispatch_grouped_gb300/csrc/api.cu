@@ -256,7 +256,8 @@ const char* moe_status_string(moe_status st) {
         case MOE_ERR_UNSUPPORTED: return "MOE_ERR_UNSUPPORTED: shape or dtype not supported";
         case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE: workspace missing, misaligned or too small";
         case MOE_ERR_CUDA: return "MOE_ERR_CUDA: a CUDA call or kernel launch failed";
-        case MOE_ERR_DEVICE_BOUNDS: return "MOE_ERR_DEVICE_BOUNDS: an id outside its range";
+        case MOE_ERR_DEVICE_BOUNDS:
+            return "MOE_ERR_DEVICE_BOUNDS: expert id outside [0, E), or token id outside [0, V)";
         case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT: a device-side wait timed out";
     }
     return "unknown moe_status";
