@@ -657,13 +657,19 @@ __global__ void __launch_bounds__(kJoinColumns * kJoinGroups) embed_join_kernel(
 }
 
 // Sorted tokens that a block sums. Long chunks leave fewer runs to join, short ones more blocks:
-// the longest of 16, 32, ... with which the blocks still fill the SMs eight deep (16384 tokens of
-// 5120 columns: 16 took 247 us, 32 239, 64 235; 8471 of 104: 19.2, 21.4 and 25.0), and at least a
-// thousandth of the tokens, so that a run over all of them is joined from a thousand parts or so.
+// of 16, 32, ... 512 the longest with which the blocks still fill the SMs eight deep (16384 tokens
+// of 5120 columns: 16 took 247 us, 32 239, 64 235; 8471 of 104: 19.2, 21.4 and 25.0), or the
+// shortest that leaves at most 1024 chunks, whichever is longer. Past 524288 tokens chunks stay at
+// 512, and a run over all tokens is joined from T / 512 parts, a quarter of them by each group of
+// threads one after the other.
+// A GB300's SMs as a number: the workspace's size goes by the chunks and must not change with the
+// device that is current.
+constexpr int kChunkSms = 152;
 int chunk_of(int T, int d) {
     const long long slices = (d + 1023) / 1024;
     int c = 16;
-    while (c < kMaxChunk && (T / (2 * c) * slices >= 8 * 152 || (long long)c * 1024 < T)) c *= 2;
+    while (c < kMaxChunk && (T / (2 * c) * slices >= 8 * kChunkSms || (long long)c * 1024 < T))
+        c *= 2;
     return c;
 }
 
@@ -716,7 +722,7 @@ cudaError_t launch_embed_backward(const void* dout, const void* ids, bool ids64,
                                        : few_kernel<512>(bf16, out_bf16, ids64);
         const long long blocks = ((long long)V + rows - 1) / rows;
         int slices = 1;  // of the columns, where the rows alone are too few blocks
-        while (blocks * slices < 4 * 152 && nv > 64 * slices) slices *= 2;
+        while (blocks * slices < 4 * device_sm_count() && nv > 64 * slices) slices *= 2;
         return launch_kernel(fn, dim3((unsigned)blocks, slices), dim3(threads), 0, s,
                              static_cast<const uint4*>(dout), ids, T, V, nv, rows, scale, d_table,
                              row_bytes, status);
