@@ -234,7 +234,9 @@ struct Share {
 // Bound by memory: 2 or 4 values of the row's type read and written for each of T d, and the
 // statistics. 16384 rows of 5120 bf16 values, root mean square: 52 us, 6.4 TB/s (0.95 of the
 // measured copy bandwidth); 4096 rows of 4096, layer norm with residual: 24.2 us, 5.6 TB/s, where
-// starting and draining count for more; 8 rows of 2048: 1.8 us, latency alone. The layer norm's
+// starting and draining count for more; 8192 rows of 2880 fp32 values, layer: 34.6 us (0.81);
+// 16384 of 512 bf16 values, a warp a row, rms: 6.0 us (0.83); 8 rows of 2048: 1.8 us, latency
+// alone. The layer norm's
 // two sums over a row are taken one after the other (the squares about the mean, so that a large
 // mean costs no precision); the second costs 2 us of those 24.2.
 // The bound on blocks holds the registers at 64 (80 where a warp takes a row): the rare second
@@ -378,7 +380,7 @@ struct NormBackwardArgs {
 // unpacked again: holding them as fp32 would cost 32 registers, and so a resident block.
 // Bound by memory (3 or 4 values for each of T d), closely followed by issue: half of all slots at
 // 16384 rows of 5120 bf16 values with a residual's gradient, 106 us with the reduction, 6.3 TB/s
-// (0.94 of the measured copy bandwidth). With scalar arithmetic and branches on the row's end it
+// (0.93 of the measured copy bandwidth). With scalar arithmetic and branches on the row's end it
 // took 200 us. Narrow rows pay more for the partial sums (4096 rows of 2048: 19 us, floor 10).
 template <typename T, int THREADS, bool RMS, bool RES>
 __global__ void __launch_bounds__(THREADS, min_blocks(THREADS, sizeof(T)))
