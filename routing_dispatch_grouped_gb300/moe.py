@@ -2,6 +2,10 @@
 CUDA kernels. Tensors are PyTorch CUDA tensors (PyTorch provides device memory and streams);
 outputs and workspaces not passed in are allocated here with torch.
 
+`stream` is the stream that a call's work is enqueued on (the current one if None). Outputs that a
+call allocates belong to the current stream whatever `stream` is, as with any PyTorch call: let the
+given stream wait for the current one first, or pass them in.
+
 The functions keep the C names: moe_route, moe_dispatch, moe_gate_up, moe_down, moe_experts,
 moe_combine, moe_forward. A non-zero status raises MoEError. There is no CPU fallback: if the
 library is missing, loading raises.
@@ -191,14 +195,15 @@ def _w_dims(w, kind):
 
 
 def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
-    """A workspace of one call. A call that does not return it names the stream it was given: the
-    block belongs to the current stream, and the allocator would hand it out again while the given
-    one still uses it."""
-    # torch's caching allocator returns blocks aligned to at least 512 bytes
-    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    """A workspace of one call. A call that does not return it names the stream it was given, so
+    that the block comes from that stream's memory: nothing orders the given stream behind the
+    current one, whose earlier work may still use a block of its own, and whose later work would be
+    given the block while the given stream still uses it."""
     if stream is not None:
-        ws.record_stream(stream)
-    return ws
+        with torch.cuda.stream(stream):
+            return _workspace(nbytes, device)
+    # torch's caching allocator returns blocks aligned to at least 512 bytes
+    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
 # ------------------------------------------------------------------------------------------------

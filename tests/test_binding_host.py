@@ -12,6 +12,20 @@ class Stream:
     cuda_stream = 0x5157
 
 
+class Current:
+    """torch.cuda.stream as far as it goes without a GPU: which stream is current."""
+    stack = [None]
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __enter__(self):
+        Current.stack.append(self.stream)
+
+    def __exit__(self, *exc):
+        Current.stack.pop()
+
+
 class Cuda:
     """As much of a contiguous CUDA tensor as the binding looks at."""
     made = 0
@@ -20,7 +34,7 @@ class Cuda:
         Cuda.made += 1
         self.shape, self.dtype, self.index = torch.Size(shape), dtype, index
         self.device = torch.device("cuda", index)
-        self.is_cuda, self.address, self.streams = True, 0x100000 * Cuda.made, []
+        self.is_cuda, self.address, self.owner = True, 0x100000 * Cuda.made, Current.stack[-1]
 
     def is_contiguous(self):
         return True
@@ -39,9 +53,6 @@ class Cuda:
 
     def get_device(self):
         return self.index
-
-    def record_stream(self, stream):
-        self.streams.append(stream)
 
 
 class Library:
@@ -77,6 +88,7 @@ def allocated(monkeypatch):
         got.append(Cuda(shape[0] if isinstance(shape[0], tuple) else shape, dtype))
         return got[-1]
     monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch.cuda, "stream", Current)
     return got
 
 
@@ -124,16 +136,20 @@ STEPS = {
 
 @pytest.mark.parametrize("call", [_norm_backward, _embed_backward, *STEPS.values()],
                          ids=["norm_backward", "embed_backward", *STEPS])
-def test_a_workspace_of_the_call_is_kept_for_the_stream_it_was_given(library, allocated, call):
-    """Nothing holds such a workspace after the call has returned, so the allocator has to know
-    that the given stream still uses it."""
+def test_a_workspace_of_the_call_belongs_to_the_stream_it_was_given(library, allocated, call):
+    """Nothing holds such a workspace after the call has returned, and nothing orders the given
+    stream behind the current one: the block has to come from the given stream's own memory, which
+    is reused in that stream's order alone."""
     stream = Stream()
     call(stream=stream)
     ws, = allocated
-    assert ws.dtype is torch.uint8 and ws.streams == [stream]
+    assert ws.dtype is torch.uint8 and ws.owner is stream and Current.stack == [None]
     name, args = library.calls[-1]
     args = [getattr(a, "value", a) for a in args]
     assert ws.address in args and args[-1] == stream.cuda_stream
+    if call in (_norm_backward, _embed_backward):
+        call()
+        assert allocated[-1].owner is None
 
 
 # ------------------------------------------------------------------------------------------------
