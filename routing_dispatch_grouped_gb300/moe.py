@@ -2,9 +2,9 @@
 CUDA kernels. Tensors are PyTorch CUDA tensors (PyTorch provides device memory and streams);
 outputs and workspaces not passed in are allocated here with torch.
 
-`stream` is the stream that a call's work is enqueued on (the current one if None). Outputs that a
-call allocates belong to the current stream whatever `stream` is, as with any PyTorch call: let the
-given stream wait for the current one first, or pass them in.
+`stream` is the stream that a call's work is enqueued on (the current one if None). A workspace that
+a call allocates belongs to it. Outputs belong to the current stream whatever `stream` is, as with
+any PyTorch call: let the given stream wait for the current one first, or pass them in.
 
 The functions keep the C names: moe_route, moe_dispatch, moe_gate_up, moe_down, moe_experts,
 moe_combine, moe_forward. A non-zero status raises MoEError. There is no CPU fallback: if the
@@ -194,14 +194,14 @@ def _w_dims(w, kind):
     return E, K, (C // 2 if kind == W_GATE_UP else C), 0
 
 
-def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
-    """A workspace of one call. A call that does not return it names the stream it was given, so
-    that the block comes from that stream's memory: nothing orders the given stream behind the
-    current one, whose earlier work may still use a block of its own, and whose later work would be
-    given the block while the given stream still uses it."""
+def _workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace of one call, from the memory of the stream that the call was given: nothing
+    orders that stream behind the current one, whose earlier work may still use a block of its own,
+    and whose later work would be given the block, once it is dropped, while the given stream still
+    uses it."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return _workspace(nbytes, device)
+            return _workspace(nbytes, device, None)
     # torch's caching allocator returns blocks aligned to at least 512 bytes
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
@@ -265,7 +265,7 @@ def moe_dispatch(topk_ids, E, x=None, workspace=None, out=None, stream=None):
     else:
         o["x_sorted"] = None
     ws = workspace if workspace is not None else _workspace(moe_dispatch_workspace_size(T, E, k),
-                                                            dev)
+                                                            dev, stream)
     _check("moe_dispatch", lib().moe_dispatch(
         _p(topk_ids), _p(x), dt, T, d, E, k, _p(o["counts"]), _p(o["offsets"]),
         _p(o["sorted_to_slot"]), _p(o["slot_to_sorted"]), _p(o["x_sorted"]), _p(ws),
@@ -373,7 +373,7 @@ def moe_forward(x, logits, w_gate_up, w_down, k, score_fn=SOFTMAX, flags=RENORMA
     w = topk_weights if topk_weights is not None else torch.empty(T, k, dtype=torch.float32,
                                                                   device=dev)
     ws = workspace if workspace is not None else _workspace(
-        moe_forward_workspace_size(T, d, E, k, I, Is, x.dtype), dev)
+        moe_forward_workspace_size(T, d, E, k, I, Is, x.dtype), dev, stream)
     _check("moe_forward", lib().moe_forward(
         _p(x), _p(logits), _dt(x), T, d, E, k, I, score_fn, flags, _p(w_gate_up), _p(w_down),
         _p(w_shared_gate_up), _p(w_shared_down), Is, _p(ids), _p(w), _p(out), _p(ws), ws.numel(),
@@ -405,7 +405,7 @@ def moe_forward_host(x_host, logits_host, w_gate_up, w_down, k, score_fn=SOFTMAX
     dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
     out = out if out is not None else torch.empty(T, d, dtype=x_host.dtype).pin_memory()
     ws = workspace if workspace is not None else _workspace(
-        moe_forward_host_workspace_size(T, d, E, k, I, Is, x_host.dtype), dev)
+        moe_forward_host_workspace_size(T, d, E, k, I, Is, x_host.dtype), dev, stream)
     _check("moe_forward_host", lib().moe_forward_host(
         _p(x_host), _p(logits_host), _dt(x_host), T, d, E, k, I, score_fn, flags,
         _p(w_gate_up), _p(w_down), _p(w_shared_gate_up), _p(w_shared_down), Is, _p(out), _p(ws),
@@ -606,7 +606,7 @@ def moe_forward_train(x, logits, w_gate_up, w_down, k, score_fn=SOFTMAX, flags=R
     w = topk_weights if topk_weights is not None else torch.empty(T, k, dtype=torch.float32,
                                                                   device=dev)
     ws = workspace if workspace is not None else _workspace(
-        moe_forward_train_workspace_size(T, d, E, k, I, Is, x.dtype), dev)
+        moe_forward_train_workspace_size(T, d, E, k, I, Is, x.dtype), dev, stream)
     _check("moe_forward_train", lib().moe_forward_train(
         _p(x), _p(logits), _dt(x), T, d, E, k, I, score_fn, flags, _p(w_gate_up), _p(w_down),
         _p(w_shared_gate_up), _p(w_shared_down), Is, _p(ids), _p(w), _p(out), _p(ws), ws.numel(),
@@ -661,7 +661,7 @@ def moe_backward(dout, x, logits, w_gate_up, w_down, k, topk_ids, topk_weights, 
     dsgu = get("d_w_shared_gate_up", (d, 2 * Is), wdt) if Is else None
     dsd = get("d_w_shared_down", (Is, d), wdt) if Is else None
     ws = workspace if workspace is not None else _workspace(
-        moe_backward_workspace_size(T, d, E, k, I, Is, dout.dtype), dev)
+        moe_backward_workspace_size(T, d, E, k, I, Is, dout.dtype), dev, stream)
     _check("moe_backward", lib().moe_backward(
         _p(dout), _p(x), _p(logits), _dt(dout), T, d, E, k, I, score_fn, flags, _p(w_gate_up),
         _p(w_down), _p(w_shared_gate_up), _p(w_shared_down), Is, _p(topk_ids), _p(topk_weights),
@@ -1136,7 +1136,7 @@ def moe_forward_mx(x, logits, w_gate_up: MxWeights, w_down: MxWeights, k, score_
     w = topk_weights if topk_weights is not None else torch.empty(T, k, dtype=torch.float32,
                                                                   device=dev)
     ws = workspace if workspace is not None else _workspace(
-        moe_forward_mx_workspace_size(T, d, E, k, I, Is), dev)
+        moe_forward_mx_workspace_size(T, d, E, k, I, Is), dev, stream)
     _check("moe_forward_mx", lib().moe_forward_mx(
         _p(x), _p(logits), T, d, E, k, I, score_fn, flags, _p(w_gate_up), _p(w_down),
         _p(w_shared_gate_up), _p(w_shared_down), Is, _p(ids), _p(w), _p(out), _p(ws), ws.numel(),
@@ -1169,7 +1169,7 @@ def moe_forward_mx_tc(x, logits, w_gate_up: MxWeights, w_down: MxWeights, k, sco
     w = topk_weights if topk_weights is not None else torch.empty(T, k, dtype=torch.float32,
                                                                   device=dev)
     ws = workspace if workspace is not None else _workspace(
-        moe_forward_mx_tc_workspace_size(T, d, E, k, I, Is), dev)
+        moe_forward_mx_tc_workspace_size(T, d, E, k, I, Is), dev, stream)
     _check("moe_forward_mx_tc", lib().moe_forward_mx_tc(
         _p(x), _p(logits), T, d, E, k, I, score_fn, flags, _p(w_gate_up), _p(w_down),
         _p(w_shared_gate_up), _p(w_shared_down), Is, _p(ids), _p(w), _p(out), _p(ws), ws.numel(),
@@ -1225,7 +1225,7 @@ def moe_gate_up_mx_tc(x_codes, x_sf, offsets, w_gate_up: MxWeights, R, h_codes, 
                       sorted_to_slot=None, topk_weights=None, scale_input=False,
                       workspace=None, stream=None):
     d, E, I = w_gate_up.K, w_gate_up.E, w_gate_up.N
-    ws = workspace if workspace is not None else _workspace(256, x_codes.device)
+    ws = workspace if workspace is not None else _workspace(256, x_codes.device, stream)
     _check("moe_gate_up_mx_tc", lib().moe_gate_up_mx_tc(
         _p(x_codes), _p(x_sf), _p(offsets), _p(sorted_to_slot), _p(topk_weights), R, d, E, I,
         _p(w_gate_up), SCALE_INPUT if scale_input else 0, _p(h_codes), _p(h_sf), _p(ws),
@@ -1236,7 +1236,7 @@ def moe_gate_up_mx_tc(x_codes, x_sf, offsets, w_gate_up: MxWeights, R, h_codes, 
 def moe_down_mx_tc(h_codes, h_sf, offsets, w_down: MxWeights, R, y_sorted, workspace=None,
                    stream=None):
     I, E, d = w_down.K, w_down.E, w_down.N
-    ws = workspace if workspace is not None else _workspace(256, h_codes.device)
+    ws = workspace if workspace is not None else _workspace(256, h_codes.device, stream)
     _check("moe_down_mx_tc", lib().moe_down_mx_tc(
         _p(h_codes), _p(h_sf), _p(offsets), R, I, E, d, _p(w_down), _p(y_sorted), _p(ws),
         ws.numel(), _stream(stream)))
