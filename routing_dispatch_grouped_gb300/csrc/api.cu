@@ -190,7 +190,7 @@ moe_status clear_status(void* workspace, cudaStream_t s) {
 }
 
 // The status word of an empty call. Such a call succeeds on any machine, so the word is written only
-// where the driver knows the workspace for device memory.
+// where CUDA knows the workspace for device memory.
 moe_status clear_status_of_empty(void* workspace, cudaStream_t s) {
     cudaPointerAttributes a;
     if (cudaPointerGetAttributes(&a, workspace) != cudaSuccess) {
